@@ -31,6 +31,34 @@ struct Half16<true> {
   }
 };
 
+// Two int8 codes (bytes of a word with 0x80 added to each) as exact f16: 0x6400 | u is 1024 + u.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t codes_f16(uint32_t biased) {
+  const uint32_t h = __byte_perm(biased, 0x64646464u, SEL);
+  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&h),
+                            __half2half2(__ushort_as_half(static_cast<unsigned short>(0x6480u))));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The same, times 2^-14, as exact bf16: the bits 0x00uu are u 2^-133 for every byte u, below the
+// normal range and in its first binade alike, and (u - 128) 2^-14 has eight bits.  So reduced, 128
+// products with a bf16 query add up inside fp32's range whatever the query's values are (128 * 128 *
+// 2^-14 = 1).
+constexpr float kCodeUnits = 16384.f;      // of a bf16 code: what a score has to be multiplied by
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t biased) {
+  const uint32_t h = __byte_perm(biased, 0u, SEL);
+  uint32_t v;                              // h * 2^119 - 128 * 2^-14
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v) : "r"(h), "r"(0x7b007b00u), "r"(0xbc00bc00u));
+  return v;
+}
+// A word's codes as operands of the queries' type.
+template <bool BF16, uint32_t SEL>
+__device__ __forceinline__ uint32_t codes16(uint32_t w) {
+  if constexpr (BF16) return codes_bf16<SEL>(w ^ 0x80808080u);
+  return codes_f16<SEL>(w ^ 0x80808080u);
+}
+
 __device__ __forceinline__ uint32_t div_fast(uint32_t n, const FastDiv& f) {
   return f.d > 1 ? static_cast<uint32_t>(__umul64hi(n, f.magic)) : n;
 }

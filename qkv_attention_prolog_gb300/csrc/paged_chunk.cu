@@ -76,15 +76,6 @@ struct Piece {
   int from;
 };
 
-// Two int8 codes (bytes of a word with 0x80 added to each) as exact f16: 0x6400 | u is 1024 + u.
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t codes_f16(uint32_t biased) {
-  const uint32_t h = __byte_perm(biased, 0x64646464u, SEL);
-  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&h),
-                            __half2half2(__ushort_as_half(static_cast<unsigned short>(0x6480u))));
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // 16 bytes, or zeros without an access; no branch, so that several are in flight.
 __device__ __forceinline__ uint4 load_or_zero(const int8_t* at, bool ok) {
   uint4 v;
@@ -97,22 +88,6 @@ __device__ __forceinline__ uint4 load_or_zero(const int8_t* at, bool ok) {
       : "l"(at), "r"(static_cast<int>(ok))
       : "memory");
   return v;
-}
-
-// Two codes of a word as exact bf16: with c = (c & 127) - (c & 128), 0x4300 | (c & 127) is 128 +
-// (c & 127), and 0x4300 | (c & 128) is 128 + (c & 128).
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t codes) {
-  const uint32_t h = __byte_perm(codes, 0x43434343u, SEL);
-  const uint32_t a = h & 0x437f437fu, b = h & 0x43804380u;
-  const __nv_bfloat162 v =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-template <bool BF16, uint32_t SEL>
-__device__ __forceinline__ uint32_t codes16(uint32_t w) {
-  if constexpr (BF16) return codes_bf16<SEL>(w);
-  return codes_f16<SEL>(w ^ 0x80808080u);
 }
 
 // Sixteen codes (piece c of row r) into an operand tile: 128-byte rows of 64 elements, two halves,
@@ -458,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------------- pages and scales
     const int64_t pitch = static_cast<int64_t>(p.Nk) * kHeadDim;
     const bool mine = lane < kRuns;        // a run each
+    const float units = BF16 ? kCodeUnits : 1.f;
     int at = 0;                            // tiles so far
     bool ok = true;
     for (int r = 0; ok && r < rounds; ++r) {
@@ -494,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float vabs = fmaxf(fabsf(vs), kTinyScale);
         const int in = t0 - static_cast<int>(div_fast(t0 >> 4, p.pg.runs)) * bs;   // row of the page
         x.off = id < 0 || id >= p.pg.block_num ? -1 : (id * bs + in) * pitch + hk * kHeadDim;
-        x.f = fmaf(ks, 0.f, ks * p.scale_log2);      // (an infinite scale gives NaN: code 0 * inf is)
+        x.f = fmaf(ks, 0.f, ks * units * p.scale_log2);  // (an infinite scale gives NaN: code 0 * inf is)
         x.lv = fmaf(vs, 0.f, __log2f(vabs));
         x.inv = __fdividef(1.f, vabs);
         x.sign = vs <= -kTinyScale ? -1.f : fabsf(vs) < kTinyScale ? 0.f : 1.f;

@@ -222,15 +222,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two int8 codes (bytes of a word with 0x80 added to each) as exact f16: 0x6400 | u is 1024 + u.
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t codes_f16(uint32_t biased) {
-  const uint32_t h = __byte_perm(biased, 0x64646464u, SEL);
-  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&h),
-                            __half2half2(__ushort_as_half(static_cast<unsigned short>(0x6480u))));
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
