@@ -9,9 +9,10 @@
 // out again in fp32.
 //
 // What bounds it is the stream of codes, 256 bytes per token and k/v head, against 4 * rows * 128
-// multiply-adds: the tensor cores' register path (mma.sync m16n8k16, f16 operands, fp32 sums) has
-// the rate for 8 or 16 rows, and its operands come from registers, where int8 becomes f16 by a byte
-// permute and one packed subtraction, exactly.  Both products run transposed, S^T = K q^T and
+// multiply-adds: the tensor cores' register path (mma.sync m16n8k16, 16-bit operands, fp32 sums) has
+// the rate for 8 or 16 rows, and its operands come from registers, where int8 becomes 16 bits by a
+// byte permute and one packed instruction, exactly: V's codes f16, K's the type of q, which enters the
+// first product as it is (scaled into f16's range, bf16 rows lost bits to the largest one beside them).  Both products run transposed, S^T = K q^T and
 // O^T = V^T P^T, so that the tokens and the channels fill the 16 rows of the instruction and the
 // query rows its 8 columns: eight rows (one token of up to eight heads) cost half of what rows as
 // the 16-row operand would, and P turns from the first product's layout to the second's by an 8x8
@@ -213,13 +214,21 @@ __device__ __forceinline__ Line lay_line(const AttnParams& p, const Parts& parts
   return l;
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <bool BF16>
+__device__ __forceinline__ void mma_16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
@@ -246,7 +255,7 @@ __device__ __forceinline__ void load_run(void* dst, const CUtensorMap* map, uint
 
 // What a step's products need of its page, worked out once by one lane.
 struct Meta {
-  float f;                                 // ks * scale * log2(e) (and q's power of two)
+  float f;                                 // ks * scale * log2(e)
   float lv;                                // log2 |vs|
   float inv;                               // 1 / |vs|
   float sign;                              // of vs; 0: vs counts as 0
@@ -558,16 +567,16 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_decode_kernel(
       ks = ok ? p.pg.k_scale[page * p.Nk + sg.hk] : 0.f;
       vs = ok ? p.pg.v_scale[page * p.Nk + sg.hk] : 0.f;
     };
-    float qscale = 0.f;                      // set once q is known
     auto put_place = [&](int i, int64_t id) {            // of this lane's step i of the batch
       const int t0 = token_of(sg, place_of(sg, warp, i));
       const int row = t0 - static_cast<int>(div_fast(t0 >> 4, p.pg.runs)) * bs;
       reinterpret_cast<int4*>(meta + (i & (2 * kBatch - 1)))[1] = make_int4(t0, check_id(id), row, 0);
     };
     auto put_scales = [&](int i) {
+      constexpr float units = BF16 ? kCodeUnits : 1.f;
       const float vabs = fmaxf(fabsf(vs), kTinyScale);
       reinterpret_cast<float4*>(meta + (i & (2 * kBatch - 1)))[0] =
-          make_float4(fmaf(ks, 0.f, ks * qscale),        // (an infinite scale gives NaN: code 0 * inf is)
+          make_float4(fmaf(ks, 0.f, ks * units * p.scale_log2),  // (an infinite scale gives NaN: code 0 * inf is)
                       fmaf(vs, 0.f, __log2f(vabs)), __fdividef(1.f, vabs),
                       vs <= -kTinyScale ? -1.f : fabsf(vs) < kTinyScale ? 0.f : 1.f);
     };
@@ -603,7 +612,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_decode_kernel(
     if (threadIdx.x == 0) next_seg(p, line, parts.inner, kRows, &cur, &segs[after]);
 
     // q rows 8t + g, the channels of this lane's k pieces: step s holds four of them
-    float qf[NT][8][4];
+    uint32_t qb[NT][8][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int row = row0 + 8 * t + g;
@@ -615,44 +624,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_decode_kernel(
       for (int h = 0; h < 4; ++h) {          // 8 channels at a time
         uint4 raw = make_uint4(0u, 0u, 0u, 0u);
         if (ok) raw = *reinterpret_cast<const uint4*>(q + h * 8);
-        const T* e = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) qf[t][h * 2 + (k >> 2)][k & 3] = H::to_f(e[k]);
+        qb[t][2 * h][0] = raw.x;
+        qb[t][2 * h][1] = raw.y;
+        qb[t][2 * h + 1][0] = raw.z;
+        qb[t][2 * h + 1][1] = raw.w;
       }
     }
-    // bf16 queries enter the f16 products scaled by a power of two that brings the tile's largest
-    // magnitude to 2^14..2^15: exact but for elements 2^-29 of it
-    float unscale = 1.f;
-    if (BF16) {
-      float m = 0.f;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m = fmaxf(m, fabsf(qf[t][s][k]));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      int e = static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14;   // m in [2^(e+14), 2^(e+15))
-      if (e < -110) e = -110;                                          // (zeros, tiny values)
-      const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      unscale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) qf[t][s][k] *= up;
-    }
-    uint32_t qb[NT][8][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        qb[t][s][0] = Half16<false>::pack(qf[t][s][0], qf[t][s][1]);
-        qb[t][s][1] = Half16<false>::pack(qf[t][s][2], qf[t][s][3]);
-      }
-    qscale = unscale * p.scale_log2;
     put_scales(lane);
     __syncwarp();
 
@@ -701,12 +678,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_decode_kernel(
           const uint4 kb = *reinterpret_cast<const uint4*>(k + 8 * 128);
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
-            const uint32_t u = word(ka, q4) ^ 0x80808080u, v = word(kb, q4) ^ 0x80808080u;
-            const uint32_t a[4] = {codes_f16<0x4140>(u), codes_f16<0x4140>(v),
-                                   codes_f16<0x4342>(u), codes_f16<0x4342>(v)};
+            const uint32_t u = word(ka, q4), v = word(kb, q4);
+            const uint32_t a[4] = {codes16<BF16, 0x4140>(u), codes16<BF16, 0x4140>(v),
+                                   codes16<BF16, 0x4342>(u), codes16<BF16, 0x4342>(v)};
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-              mma_f16(s[t][h], a, qb[t][half * 4 + q4][0], qb[t][half * 4 + q4][1]);
+              mma_16<BF16>(s[t][h], a, qb[t][half * 4 + q4][0], qb[t][half * 4 + q4][1]);
           }
         }
       }
@@ -800,8 +777,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_decode_kernel(
                                   codes_f16<0x4140>(cd1), codes_f16<0x4342>(cd1)};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            mma_f16(o[t][q4 * 2], a0, pb[t][h][0], pb[t][h][1]);
-            mma_f16(o[t][q4 * 2 + 1], a1, pb[t][h][0], pb[t][h][1]);
+            mma_16<false>(o[t][q4 * 2], a0, pb[t][h][0], pb[t][h][1]);
+            mma_16<false>(o[t][q4 * 2 + 1], a1, pb[t][h][0], pb[t][h][1]);
           }
         }
       }

@@ -1,16 +1,19 @@
 """GPU parity of the attention operators where queries, scales or values are far from ordinary: rows
 of a tile that differ by orders of magnitude, infinities and NaN that some rows see and others do
 not.  Each case names the kernel that it is meant for."""
+import numpy as np
 import pytest
 import torch
 
+import oracle
 import qkv_attention_prolog_gb300 as pkg
-from tests.attention_util import D, SCALE, ragged, to_dev
+from tests.attention_util import (D, SCALE, assert_within, attn_tolerance, ragged, run_paged, to_dev)
+from tests.gpu_util import f64
 from tests.test_gpu_attention import _check_paged
 
 pytestmark = pytest.mark.gpu
 
-BF = torch.bfloat16
+BF, FP = torch.bfloat16, torch.float16
 FEW = 256 + 2 * 504 * 16 * (D + 2) * 4                # workspaces: parts of few rows, of key tiles
 TILES = 256 + 2 * 160 * 2 * 128 * (D + 2) * 4
 
@@ -27,11 +30,70 @@ def _takes(d, max_new, size):
     assert pkg.mlap_paged_attention_get_workspace_size(a) == size
 
 
+def _oracle_paged(t, scale=SCALE, window=0, sinks=0):
+    with np.errstate(invalid="ignore"):
+        return oracle.paged_attention(f64(t["q"]), t["k_cache"].numpy(), t["v_cache"].numpy(),
+                                      t["k_scale"].numpy(), t["v_scale"].numpy(),
+                                      t["cu_seqlens"].numpy(), t["context_lens"].numpy(),
+                                      t["block_table"].numpy(), scale, window, sinks)
+
+
+def _keys(t):
+    return int((t["context_lens"] + t["cu_seqlens"].diff()).max())
+
+
 # new tokens, Nq, Nk, workspace: a tile of eight rows, of sixteen, of 128
 SHAPES = [(1, 16, 2, FEW), (4, 8, 2, FEW), (70, 8, 2, TILES)]
 
 
 # ---------------------------------------------------------------------------------------- queries
+@pytest.mark.parametrize("new,Nq,Nk,size", SHAPES)
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("loud", [float("inf"), float("nan"), 2.0 ** 40, 2.0 ** 13])
+def test_paged_rows_do_not_depend_on_each_other(new, Nq, Nk, size, dtype, loud):
+    # one row of a tile holds an infinity, a NaN or values far above the others': the others' outputs
+    # are those of their own scores
+    if loud == 2.0 ** 40 and dtype == FP:
+        pytest.skip("no fp16 value")
+    t = ragged([new, new], [90, 333], 16, Nk, Nq, dtype, seed=61)
+    ordinary = f64(t["q"]).copy()
+    if np.isfinite(loud):
+        t["q"][0, 1] = (t["q"][0, 1].float() * loud).to(dtype)
+    else:
+        t["q"][0, 1, 9] = loud
+    ordinary[0, 1] = 0.0
+    ref = _oracle_paged(t)
+    d = to_dev(t)
+    _takes(d, new, size)
+    assert run_paged(d, new) == 0
+    kmax = 127.0 * float(t["k_scale"].max())
+    tol = attn_tolerance(ref, None, np.abs(ordinary).max() * kmax * D * SCALE, dtype, FP, _keys(t))
+    rows = slice(0, int(t["cu_seqlens"][-1]))
+    got, want, tol = f64(d["out"])[rows].copy(), ref["out"][rows].copy(), tol[rows]
+    assert np.isnan(got[0, 1]).all() if not np.isfinite(loud) else np.isfinite(got[0, 1]).all()
+    got[0, 1] = want[0, 1] = tol[0, 1] = 0.0
+    assert_within(got, want, tol, "the other rows")
+
+
+@pytest.mark.parametrize("new,Nq,Nk,size", SHAPES)
+@pytest.mark.parametrize("dtype,big", [(BF, 2.0 ** 60), (FP, 60000.0)])
+def test_paged_elements_of_a_row_that_differ_widely(new, Nq, Nk, size, dtype, big):
+    # a channel of q far above the others meets keys whose codes are all 0 there: it adds nothing
+    t = ragged([new, new], [90, 333], 16, Nk, Nq, dtype, seed=62)
+    t["q"][:, :, 70] = 0.0
+    top = float(np.abs(f64(t["q"])).max())
+    t["q"][:, :, 70] = big
+    t["k_cache"][..., 70] = 0
+    ref = _oracle_paged(t)
+    d = to_dev(t)
+    _takes(d, new, size)
+    assert run_paged(d, new) == 0
+    kmax = 127.0 * float(t["k_scale"].max())
+    tol = attn_tolerance(ref, None, top * kmax * D * SCALE, dtype, FP, _keys(t))
+    rows = slice(0, int(t["cu_seqlens"][-1]))
+    assert_within(f64(d["out"])[rows], ref["out"][rows], tol[rows], "out")
+
+
 @pytest.mark.parametrize("new,Nq,Nk,size", SHAPES)
 @pytest.mark.parametrize("up", [3e35, 3e-33])
 def test_paged_queries_at_the_ends_of_the_range(new, Nq, Nk, size, up):
