@@ -105,3 +105,29 @@ def test_paged_queries_at_the_ends_of_the_range(new, Nq, Nk, size, up):
     assert bool(torch.isfinite(t["q"]).all()) and float(t["k_scale"].min()) > 1.2e-38
     _takes(to_dev(t), new, size)
     _check_paged(t, new)
+
+
+# ----------------------------------------------------------------------------------------- scales
+@pytest.mark.parametrize("new,ctx,window,size", [(2, 95, 81, FEW), (12, 90, 85, FEW), (20, 90, 85, TILES)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("name", ["k_scale", "v_scale"])
+def test_paged_bad_scale_between_the_rows_of_a_tile(new, ctx, window, size, dtype, name):
+    # page 6 holds positions 96..111, which a tile's later rows alone see; page 0's last position
+    # leaves the window of its later rows
+    for bad, page in ((float("nan"), 6), (float("inf"), 6), (-float("inf"), 6), (float("nan"), 0)):
+        t = ragged([new, new], [ctx, 33], 16, 2, 8, dtype, seed=64)
+        t[name][t["block_table"][0, page]] = bad
+        _takes(to_dev(t), new, size)
+        _check_paged(t, new, window if page == 0 else 0, 0, nonfinite=True)
+
+
+@pytest.mark.parametrize("new,size", [(1, FEW), (12, FEW), (20, TILES)])
+@pytest.mark.parametrize("name", ["k_scale", "v_scale"])
+@pytest.mark.parametrize("page", [0, 700, 1249])
+def test_paged_bad_scale_of_one_head_in_one_part(new, size, name, page):
+    # of a context that several blocks share: the rows of the other head join parts without it
+    for bad in (float("nan"), float("inf")):
+        t = ragged([new], [20000], 16, 2, 8, BF, seed=65)
+        t[name][t["block_table"][0, page], 1] = bad
+        _takes(to_dev(t), new, size)
+        _check_paged(t, new, nonfinite=True)
