@@ -512,7 +512,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = blk.tok0 + i * tpt + row_tok, pos = blk.s.ctx + tok;
       const int pos_lo = blk.pos0 + i * tpt + warp_lo, pos_hi = blk.pos0 + i * tpt + warp_hi;
       const Seen seen(p, blk, pos_lo, pos_hi);
-      float m = -INFINITY, l = 0.f;
+      // (rows of no token hold what is left in shared memory: they never raise m, which is their warp's
+      // decision for all of its rows)
+      const bool mine = row < group * tpt && tok < blk.s.len;
+      float m = mine ? -INFINITY : INFINITY, l = 0.f;
       for (int j = 0; j < blk.steps; ++j, ++done, ++at) {
         ok = warp_wait(&bar->s_full[i], done & 1, abort_flag);
         if (!ok) break;
@@ -631,7 +634,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- out = O / l; zeros for a row that saw nothing (a NaN sum stays NaN)
-      const bool mine = row < group * tpt && tok < blk.s.len;
       const int h = hk * group + row_head;
       uint4* dst = reinterpret_cast<uint4*>(
           static_cast<T*>(p.out) + ((blk.s.row0 + tok) * p.Nq + h) * kHeadDim);

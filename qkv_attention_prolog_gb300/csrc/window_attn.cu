@@ -423,7 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = tile_tok + row_tok;
       const int tok_lo = tile_tok + warp_lo, tok_hi = tile_tok + warp_hi;
       const Seen seen(p, blk, tok_lo, tok_hi);
-      float m = -INFINITY, l = 0.f;
+      // (rows of no token hold what is left in shared memory: they never raise m, which is their warp's
+      // decision for all of its rows)
+      float m = row < group * tpt && tok < plan.len ? -INFINITY : INFINITY, l = 0.f;
       for (int j = 0; j < plan.steps; ++j, ++done) {
         ok = warp_wait(&bar->s_full[i], done & 1, abort_flag);
         if (!ok) break;

@@ -7,7 +7,8 @@ import torch
 
 import oracle
 import qkv_attention_prolog_gb300 as pkg
-from tests.attention_util import (D, SCALE, assert_within, attn_tolerance, ragged, run_paged, to_dev)
+from tests.attention_util import (D, SCALE, assert_within, attn_tolerance, prompts, ragged, run_paged,
+                                  run_window, to_dev)
 from tests.gpu_util import f64
 from tests.test_gpu_attention import _check_paged
 
@@ -131,3 +132,35 @@ def test_paged_bad_scale_of_one_head_in_one_part(new, size, name, page):
         t[name][t["block_table"][0, page], 1] = bad
         _takes(to_dev(t), new, size)
         _check_paged(t, new, nonfinite=True)
+
+
+# ------------------------------------------------------------------------------- rows of no token
+def _loud(rows, loud):
+    return rows.normal_(generator=torch.Generator(device="cuda").manual_seed(3)).mul_(1e4) if loud else rows.zero_()
+
+
+@pytest.mark.parametrize("kind", ["window", "paged"])
+def test_rows_of_no_token_do_not_reach_the_others_bits(kind):
+    # groups of three heads fill 126 of a tile's 128 rows: the last two hold what an earlier call (of
+    # whole tiles) left in shared memory, and those behind a sequence's end whatever lies behind it
+    Nk, sms = 8, torch.cuda.get_device_properties(0).multi_processor_count
+    if kind == "window":
+        full, t = to_dev(prompts([256] * 24, Nk, Nk, BF, seed=70)), prompts([1000, 1333], Nk, 3 * Nk, BF, seed=71, pad=100)
+        run, longest, rows_full = run_window, 1333, 256
+    else:
+        full = to_dev(ragged([256] * 24, [900] * 24, 64, Nk, Nk, BF, seed=72))
+        t = ragged([150] * 20, [1500 - 11 * b for b in range(20)], 64, Nk, 3 * Nk, BF, seed=73, pad=100)
+        run, longest, rows_full = run_paged, 150, 256
+        _takes(to_dev(t), longest, TILES)
+    assert 24 * Nk > sms                              # a block of 256 rows for each SM
+    d = to_dev(t)
+    end = int(t["cu_seqlens"][-1])
+    got = []
+    for loud in (False, True, False, True):
+        _loud(full["q"], loud)
+        _loud(d["q"][end:], loud)
+        assert run(full, rows_full) == 0
+        assert run(d, longest) == 0
+        got.append(d["out"][:end].clone())
+    for other in got[1:]:
+        assert torch.equal(got[0].view(torch.int16), other.view(torch.int16))
