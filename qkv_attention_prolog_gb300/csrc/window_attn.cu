@@ -36,8 +36,11 @@
 //
 // Rows behind the sequence's end in its last tile of V are set to zero before the product.  Where V
 // holds infinities or NaN at positions that some rows of a tile see and others do not, 0 * inf
-// spoils the others: a row whose result is not finite is worked out again by its warp, key by key.
-#include "attn_row.cuh"
+// spoils the others: items with a row whose weights are finite and whose result is not are marked,
+// and the CTA goes through them once more, with care: what is not finite is cleared from the tiles of
+// V before the products, and comes to the rows that see it at the end (8192 tokens: 360 us, with one
+// NaN in V 1120, V all NaN 1380; rows worked out again key by key took 299 ms).  A row that sees
+// a NaN in K has no finite weights, and stays as it is.
 #include "attn_tile.cuh"
 
 namespace mlap {
@@ -48,8 +51,24 @@ constexpr int kThreads = 384;
 constexpr int kPlans = 4;                  // items worked out ahead
 constexpr int kReaders = 10;               // warps that read a plan
 constexpr int kStage = 32 * 128;           // a softmax warp's rows, half of their columns in 16 bits
+constexpr int kMarks = 256;                // items whose marks are kept (the others share them)
+// Key tiles of an item that some of its rows do not see whole: the 255 positions behind its first row,
+// and as many in front of the windows, with up to seven columns behind the sinks, in tiles of 128.
+constexpr int kPartly = 8;
+
+// Items to go through with care, and what such an item's tiles of V held that is not finite, each word
+// or byte by one of tile 0's softmax warps.
+struct Care {
+  uint64_t noted, read;                    // by these warps; by all eight
+  uint32_t marks[2 * kMarks / 32];         // of items' tiles
+  uint32_t marked;                         // any
+  int32_t column[kPartly];                 // where the tiles begin that some rows do not see whole
+  uint32_t keys[kPartly][kTile / 32];      // their keys with values that are not finite
+  uint8_t kinds[4][3][kHeadDim / 8];       // channels with infinities, negative ones, NaN in the others
+};
 constexpr int kSmemBytes = (2 + 2 * kStages) * kOperand + 8 * kStage + 1024 + 256 + kPlans * 64 +
-                           (kCountedSeqs + 1) * 4;
+                           static_cast<int>(sizeof(Care)) + (kCountedSeqs + 1) * 4;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
 struct Bars {
   uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
@@ -66,125 +85,255 @@ struct __align__(16) Plan {
   int32_t len, hk;
   int32_t tok0, tiles, steps, valid;       // tiles 0: no further item; valid: columns of the last step
   int32_t sink_end, sink_cols, shift, from;          // from: the first of the item's steps
-  TilePart part;
+  TilePart part;                           // (with care the item is whole; first: bits of marked tiles)
 };
 static_assert(sizeof(Plan) == 64, "four 16-byte reads");
 
+struct Smem {
+  uint8_t *q, *k, *v;                      // two Q tiles, the stages of K and V
+  Bars* bar;
+  Plan* plans;
+  uint8_t* staged;
+  Care* care;
+  int* first;
+};
+__device__ __forceinline__ Smem smem_of(uint8_t* raw) {
+  const uint32_t at = smem_u32(raw);
+  Smem s;
+  s.q = raw + (((at + 1023u) & ~1023u) - at);
+  s.k = s.q + 2 * kOperand;
+  s.v = s.k + kStages * kOperand;
+  s.bar = reinterpret_cast<Bars*>(s.v + kStages * kOperand);
+  s.plans = reinterpret_cast<Plan*>(s.v + kStages * kOperand + 256);
+  s.staged = reinterpret_cast<uint8_t*>(s.plans + kPlans);
+  s.care = reinterpret_cast<Care*>(s.staged + 8 * kStage);
+  s.first = reinterpret_cast<int*>(s.care + 1);
+  return s;
+}
+
+// What a CTA takes of the items.  Whole ones, a round of one for each CTA at a time, there and back;
+// fewer items than CTAs are shared by key tiles where that pays, and what is left after whole rounds
+// where a window keeps the items alike (16384 tokens of one k/v head, window 4096: 110 us, shared 100).
+// Without one the rounds' long items even out with the short ones left (8192 tokens of two k/v heads
+// 106 us, shared 132).
+struct Items {
+  int items, whole, shared;                // rounds of whole ones; what is left
+  bool counted, split;
+  int share, lo, hi, t_lo, place;          // the stretch; its first item and where it begins
+};
+
+__device__ __forceinline__ Block block_at(const AttnParams& p, const Smem& sm, bool counted, int tpt, int at,
+                                          int* hk, SeqRows* s) {      // of item `at`; no tiles: there is none
+  *hk = at % p.Nk;
+  const int block = at / p.Nk;
+  const int b = counted ? seq_of_block(sm.first, p.rag.B, block) : block % p.rag.B;
+  const int index = counted ? block - sm.first[b] : block / p.rag.B;
+  *s = seq_rows(p.rag, b);
+  return index < blocks_of(*s, tpt) ? block_of(p, *s, index, tpt, 0x7fffffff, 1, 8) : Block{};
+}
+
+// All threads of the CTA.
+__device__ __forceinline__ Items items_of(const AttnParams& p, const Smem& sm, int tpt, int most, bool may_split) {
+  Items it;
+  const int ctas = gridDim.x;
+  it.counted = p.rag.B <= kCountedSeqs;
+  it.items = it.counted ? sm.first[p.rag.B] * p.Nk : most;
+  it.whole = it.items / ctas;
+  it.shared = it.items - it.whole * ctas;
+  it.split = false;
+  it.share = 1;
+  it.lo = it.hi = it.t_lo = it.place = 0;
+  const bool even = p.window > 0 && 4 * static_cast<int64_t>(p.window) <= p.rag.max_new;
+  if (may_split && (it.whole == 0 || even) && it.shared > 0) {
+    int* line = reinterpret_cast<int*>(sm.staged);        // (for the moment)
+    int hk;
+    SeqRows s;
+    Block k{};
+    if (static_cast<int>(threadIdx.x) < it.shared) {
+      k = block_at(p, sm, it.counted, tpt, it.whole * ctas + threadIdx.x, &hk, &s);
+      line[threadIdx.x + 1] = k.tiles > 0 ? k.steps + kGap : 0;
+    }
+    if (threadIdx.x == 0) line[0] = sm.bar->last[0] = 0;
+    __syncthreads();
+    if (k.steps > 0) atomicMax(&sm.bar->last[0], k.steps);
+    if (threadIdx.x >> 5 == 2) sum_line(line, it.shared);
+    __syncthreads();
+    const int total = line[it.shared];
+    it.share = stretch_of(total, sm.bar->last[0], ctas, &it.split);
+    if (static_cast<int>(blockIdx.x) * it.share < total) {
+      it.lo = blockIdx.x * it.share;
+      it.hi = min(it.lo + it.share, total);
+      it.t_lo = seq_of_block(line, it.shared, it.lo);
+      it.place = line[it.t_lo];
+    }
+    __syncthreads();
+  }
+  return it;
+}
+
+// w * f + acc for two 16-bit values.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
-    window_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
-                       const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV,
-                       const __grid_constant__ CUtensorMap tmK8,
-                       const __grid_constant__ CUtensorMap tmV8, const AttnParams p, int tpt,
-                       int most, int may_split, float* slots, uint32_t* arrived) {
+__device__ __forceinline__ uint32_t fma_16x2(uint32_t w, uint32_t f, uint32_t acc) {
+  uint32_t d;
+  if constexpr (BF16) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(f), "r"(acc));
+  } else {
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(f), "r"(acc));
+  }
+  return d;
+}
+
+struct Maps {
+  const CUtensorMap *q, *k, *v, *k8, *v8;
+};
+
+// What a role has counted: plans, Q tiles, steps, steps of its own tile.
+struct Past {
+  int plans, items, steps, own;
+};
+
+// Whether every row at positions pos_lo .. pos_hi of a block sees the whole tile from column u on.
+__device__ __forceinline__ bool seen_by_all(const AttnParams& p, const Block& k, int pos_lo, int pos_hi, int u) {
+  const Seen seen(p, k, pos_lo, pos_hi);
+  const bool sinks = k.sink_cols > 0 ? u + kTile <= k.sink_end : u + kTile <= p.sinks && u + kTile - 1 <= seen.to;
+  return sinks || seen.all(u, kTile);
+}
+
+// Clears what is not finite from 32 rows of a tile of V.  Returns a word of the rows that held any, and
+// adds their kinds to the lane's channels 8 (lane & 15) .. + 7: bytes of infinities, negative ones, NaN.
+template <bool BF16>
+__device__ __noinline__ uint32_t clear_rows(uint8_t* rows, uint32_t* kinds, int lane) {
+  constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
+  uint8_t* at = rows + ((lane >> 3) & 1) * kHalf + (lane >> 4) * 128;
+  uint32_t found = 0u;
+#pragma unroll 1
+  for (int k0 = 0; k0 < 16; k0 += 4) {     // two rows at a time
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = 2 * (k0 + k);
+      v[k] = *reinterpret_cast<const uint4*>(at + r * 128 + (((lane & 7) ^ ((r + (lane >> 4)) & 7)) << 4));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = 2 * (k0 + k);
+      uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, odd[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) odd[i] = __vcmpeq2(w[i] & (kExp * 0x10001u), kExp * 0x10001u);
+      const bool any = (odd[0] | odd[1] | odd[2] | odd[3]) != 0u;
+      const uint32_t lanes = __ballot_sync(0xffffffffu, any);
+      found |= (lanes & 0xffffu ? 1u << r : 0u) | (lanes >> 16 ? 2u << r : 0u);
+      if (!any) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t nan = odd[i] & ~__vcmpeq2(w[i] & 0x7fff7fffu, kExp * 0x10001u);
+        const uint32_t neg = w[i] >> 15 & 0x00010001u, is = odd[i] & 0x00010001u, n = nan & 0x00010001u;
+        const uint32_t bits = (is & ~n & ~neg) | (is & ~n & neg) << 8;           // of the low value, and high
+        *kinds |= ((bits & 0x101u) | n << 16 & 0x10000u) << (2 * i) | (bits >> 16 | n & 0x10000u) << (2 * i + 1);
+        w[i] &= ~odd[i];
+      }
+      *reinterpret_cast<uint4*>(at + r * 128 + (((lane & 7) ^ ((r + (lane >> 4)) & 7)) << 4)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  fence_proxy_async_shared();
+  return found;
+}
+
+// Brings what clear_rows found in an item to a row's O in tensor memory (at `to`).  A warp's 32 rows;
+// row: whether the lane has one, at position pos; partly: tiles that some rows do not see whole.
+template <bool BF16>
+__device__ __noinline__ void add_cleared(const AttnParams& p, const Block& blk, const Care* care, int partly,
+                                         const void* v_head, bool row, int pos, uint32_t to) {
   using H = Half16<BF16>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint8_t* sq = smem;                                // two Q tiles
-  uint8_t* sk = sq + 2 * kOperand;
-  uint8_t* sv = sk + kStages * kOperand;
-  Bars* bar = reinterpret_cast<Bars*>(sv + kStages * kOperand);
-  Plan* plans = reinterpret_cast<Plan*>(sv + kStages * kOperand + 256);
-  uint8_t* staged = reinterpret_cast<uint8_t*>(plans + kPlans);
-  int* first = reinterpret_cast<int*>(staged + 8 * kStage);
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {            // 16 channels at a time
+    uint32_t raw[16];
+    float o[16];
+    tmem_ld_32x32b_x16(to + q * 16, raw);
+    tmem_ld_wait();
+    uint32_t kind[3] = {0u, 0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 12; ++k) kind[k % 3] |= reinterpret_cast<const uint16_t*>(care->kinds[k / 3][k % 3])[q];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      o[e] = __uint_as_float(raw[e]);
+      if ((kind[0] >> e) & 1u) o[e] += INFINITY;
+      if ((kind[1] >> e) & 1u) o[e] -= INFINITY;
+      if ((kind[2] >> e) & 1u) o[e] = NAN;
+    }
+    // Values that the row sees, so small that finite ones never add up to an infinity: four keys at a
+    // time, which a warp's rows look at together, until nothing but NaN is left.
+    constexpr uint32_t kSmall = BF16 ? 0x0d800d80u : 0x04000400u, kInf = BF16 ? 0x7f807f80u : 0x7c007c00u;
+    uint32_t sum[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    bool closed = false;
+    for (int d = 0; d < partly && !closed; ++d) {
+      for (int w = 0; w < kTile / 32 && !closed; ++w) {
+        const int u = care->column[d] + 32 * w;
+        const uint32_t mine = row ? care->keys[d][w] & sees(p, blk, pos, u) : 0u;
+        for (uint32_t rest = __reduce_or_sync(0xffffffffu, mine); rest != 0u && !closed;) {
+          uint4 x[4][2];
+          uint32_t bit[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            bit[k] = rest & (0u - rest);
+            rest ^= bit[k];
+            if (bit[k] == 0u) continue;
+            const int64_t key = key_of(blk, u + __ffs(bit[k]) - 1);
+            const uint4* at = reinterpret_cast<const uint4*>(
+                static_cast<const typename H::T*>(v_head) + key * p.Nk * kHeadDim) + 2 * q;
+            x[k][0] = at[0];
+            x[k][1] = at[1];
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if ((mine & bit[k]) == 0u) continue;
+            const uint32_t v[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w,
+                                   x[k][1].x, x[k][1].y, x[k][1].z, x[k][1].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] = fma_16x2<BF16>(v[e], kSmall, sum[e]);
+          }
+          uint32_t nan = ~0u;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) nan &= __vcmpgtu2(sum[e] & 0x7fff7fffu, kInf);
+          closed = __all_sync(0xffffffffu, !row || nan == ~0u);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float f = H::to_f(reinterpret_cast<const typename H::T*>(sum)[e]);
+      if (!(fabsf(f) < INFINITY)) o[e] += f;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) raw[e] = __float_as_uint(o[e]);
+    tmem_st_32x32b_x16(to + q * 16, raw);
+  }
+  tmem_st_wait();
+}
+
+// The CTA's items, or (CARE) the marked ones of them once more, whole whatever their parts were.  The
+// pipelines run on from one walk to the next.
+template <bool BF16, bool CARE>
+__device__ __forceinline__ Past walk(const Maps& maps, const AttnParams& p, const Smem& sm, const Items& it, int tpt,
+                                     float* slots, uint32_t* arrived, Past past) {
+  using H = Half16<BF16>;
+  Bars* bar = sm.bar;
+  Care* care = sm.care;
+  uint8_t *sq = sm.q, *sk = sm.k, *sv = sm.v;
   volatile int* abort_flag = &bar->abort;
   // (the shuffle tells the compiler that the warp's index is the same for all its lanes)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int group = p.Nq / p.Nk;
-
-  if (warp == 0 && lane == 0) {
-    prefetch_tmap(&tmQ);
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
-    mbar_init(&bar->q_full, 1);
-    mbar_init(&bar->q_empty, 1);
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&bar->k_full[i], 1);
-      mbar_init(&bar->k_empty[i], 1);
-      mbar_init(&bar->v_full[i], 1);
-      mbar_init(&bar->v_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar->s_full[i], 1);
-      mbar_init(&bar->p_full[i][0], kTile);
-      mbar_init(&bar->p_full[i][1], kTile);
-      mbar_init(&bar->o_done[i], 1);
-      mbar_init(&bar->parted[i], kTile);
-    }
-    mbar_init(&bar->drain, 1);
-    for (int i = 0; i < kPlans; ++i) {
-      mbar_init(&bar->plan_full[i], 1);
-      mbar_init(&bar->plan_empty[i], kReaders);
-    }
-    bar->abort = 0;
-    fence_mbarrier_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(&bar->tmem, 512);
-    tmem_relinquish();
-  }
-  grid_dependency_wait();
-  const bool counted = p.rag.B <= kCountedSeqs;
-  if (counted) count_blocks(p.rag, tpt, first);
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
   const uint32_t tmem = uniform(bar->tmem);
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < p.rag.B; i += kThreads)
-      if (seq_rows(p.rag, i).bad) atomicOr(p.err, kErrIndexRange);
-
-  // Whole items, a round of one for each CTA at a time, there and back; fewer items than CTAs are
-  // shared by key tiles where that pays, and what is left after whole rounds where a window keeps the
-  // items alike (16384 tokens of one k/v head, window 4096: 110 us, shared 100).  Without one the
-  // rounds' long items even out with the short ones left (8192 tokens of two k/v heads 106 us, shared
-  // 132).
-  const int items = counted ? first[p.rag.B] * p.Nk : most;
-  const int ctas = gridDim.x, whole = items / ctas, shared = items - whole * ctas;
-  auto block_at = [&](int at, int* hk, SeqRows* s) {      // of item `at`; no tiles: there is none
-    *hk = at % p.Nk;
-    const int block = at / p.Nk;
-    const int b = counted ? seq_of_block(first, p.rag.B, block) : block % p.rag.B;
-    const int index = counted ? block - first[b] : block / p.rag.B;
-    *s = seq_rows(p.rag, b);
-    return index < blocks_of(*s, tpt) ? block_of(p, *s, index, tpt, 0x7fffffff, 1, 8) : Block{};
-  };
-  bool split = false;
-  int share = 1, lo = 0, hi = 0, t_lo = 0, place = 0;     // the stretch; its first item and where it begins
-  const bool even = p.window > 0 && 4 * static_cast<int64_t>(p.window) <= p.rag.max_new;
-  if (may_split && (whole == 0 || even) && shared > 0) {
-    int* line = reinterpret_cast<int*>(staged);           // (for the moment)
-    int hk;
-    SeqRows s;
-    Block k{};
-    if (static_cast<int>(threadIdx.x) < shared) {
-      k = block_at(whole * ctas + threadIdx.x, &hk, &s);
-      line[threadIdx.x + 1] = k.tiles > 0 ? k.steps + kGap : 0;
-    }
-    if (threadIdx.x == 0) line[0] = bar->last[0] = 0;
-    __syncthreads();
-    if (k.steps > 0) atomicMax(&bar->last[0], k.steps);
-    if (warp == 2) sum_line(line, shared);
-    __syncthreads();
-    const int total = line[shared];
-    share = stretch_of(total, bar->last[0], ctas, &split);
-    if (static_cast<int>(blockIdx.x) * share < total) {
-      lo = blockIdx.x * share;
-      hi = min(lo + share, total);
-      t_lo = seq_of_block(line, shared, lo);
-      place = line[t_lo];
-    }
-    __syncthreads();
-  }
 
   // The n-th item of this CTA; null: there is none, or a wait gave up.  Every role walks the items
   // alike; the pipelines run on from one to the next.  Each reads what it needs and hands the plan
   // back: what is done once per item is code that the caches have dropped since the last one.
   auto take = [&](int n) -> const Plan* {
     if (!warp_wait(&bar->plan_full[n % kPlans], (n / kPlans) & 1, abort_flag)) return nullptr;
-    const Plan* at = &plans[n % kPlans];
+    const Plan* at = &sm.plans[n % kPlans];
     return uniform(at->tiles) > 0 ? at : nullptr;
   };
   auto give_back = [&](int n) {
@@ -194,26 +343,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 2) {
     // -------------------------------------------------------------------- items
-    int n = 0;
+    int n = past.plans;
     auto put = [&](const Plan& plan) {
       if (!warp_wait(&bar->plan_empty[n % kPlans], ((n / kPlans) & 1) ^ 1, abort_flag)) return false;
       if (lane == 0) {
-        plans[n % kPlans] = plan;
+        sm.plans[n % kPlans] = plan;
         mbar_arrive(&bar->plan_full[n % kPlans]);
       }
       ++n;
       return true;
     };
     bool ok = true;
-    const int rounds = whole + (shared > 0 && !split);
+    const int rounds = it.whole + (it.shared > 0 && !it.split), ctas = gridDim.x;
+    int next = it.t_lo, place = it.place, number = 0;
     for (int r = 0; ok; ++r) {
       const bool part = r >= rounds;
-      if (part && (!split || place >= hi)) break;
-      const int at = part ? whole * ctas + t_lo++ : dealt(r);
-      if (at >= items) continue;
+      if (part && (!it.split || place >= it.hi)) break;
+      const int at = part ? it.whole * ctas + next++ : dealt(r);
+      if (at >= it.items) continue;
       Plan plan{};
       SeqRows s;
-      const Block k = block_at(at, &plan.hk, &s);
+      const Block k = block_at(p, sm, it.counted, tpt, at, &plan.hk, &s);
       if (k.tiles == 0) continue;
       plan.row0 = s.row0;
       plan.len = s.len;
@@ -226,22 +376,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       plan.shift = k.shift;
       plan.part.parts = 1;
       if (part) {
-        const int a0 = place + kGap, to = min(hi - a0, k.steps);
+        const int a0 = place + kGap, from = max(it.lo - a0, 0), to = min(it.hi - a0, k.steps);
         place = a0 + k.steps;
-        plan.from = max(lo - a0, 0);
-        plan.steps = to - plan.from;
-        if (plan.steps <= 0) continue;     // nothing but empty places
-        if (to < k.steps) plan.valid = kTile;
-        plan.part = part_of(a0, k.steps, share, static_cast<int>(blockIdx.x));
+        if (to - from <= 0) continue;      // nothing but empty places
+        if (!CARE) {
+          plan.from = from;
+          plan.steps = to - from;
+          if (to < k.steps) plan.valid = kTile;
+          plan.part = part_of(a0, k.steps, it.share, static_cast<int>(blockIdx.x));
+        }
+      }
+      if (CARE) {                          // tiles that this CTA wrote and marked
+        const int mark = number++ % kMarks;
+        plan.part.first = (care->marks[mark >> 4] >> (2 * (mark & 15))) & 3u;
+        if (plan.part.first == 0) continue;
       }
       ok = put(plan);
     }
     if (ok) put(Plan{});                   // the end
+    past.plans = n;
   } else if (warp == 0) {
     // -------------------------------------------------------------------- loads
-    int nq = 0, nk = 0, nv = 0;            // tiles requested so far
+    int n = past.plans, nq = past.items, nk = past.steps, nv = nk;       // tiles requested so far
     bool ok = true;
-    for (int n = 0; ok; ++n) {
+    for (; ok; ++n) {
       const Plan* at = take(n);
       if (at == nullptr) break;
       const Plan plan = *at;
@@ -256,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&bar->q_full, plan.tiles * 2 * group * tpt * 128);
         for (int i = 0; i < plan.tiles; ++i)
           for (int h = 0; h < 2; ++h)
-            tma_load_3d(sq + i * kOperand + h * kHalf, &tmQ, &bar->q_full, h * 64, hk * group,
+            tma_load_3d(sq + i * kOperand + h * kHalf, maps.q, &bar->q_full, h * 64, hk * group,
                         row0 + plan.tok0 + i * tpt);
       }
       ++nq;
@@ -280,14 +438,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         ok = warp_wait(&bar->k_empty[st], ph, abort_flag);
         if (!ok) break;
-        if (lane == 0) load(sk + st * kOperand, &tmK, &tmK8, &bar->k_full[st]);
+        if (lane == 0) load(sk + st * kOperand, maps.k, maps.k8, &bar->k_full[st]);
         ++nk;
         ok = warp_wait(&bar->v_empty[st], ph, abort_flag);
         if (!ok) break;
-        if (lane == 0) load(sv + st * kOperand, &tmV, &tmV8, &bar->v_full[st]);
+        if (lane == 0) load(sv + st * kOperand, maps.v, maps.v8, &bar->v_full[st]);
         ++nv;
       }
     }
+    give_back(n);                          // (the end)
+    past = Past{n + 1, nq, nv, 0};
     if (*abort_flag && lane == 0) {
       // give up cleanly: what was requested lands before the CTA exits (bounded)
       const uint64_t t0 = globaltimer_ns();
@@ -320,10 +480,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                        (h | k) ? 1u : 0u);
       umma_commit(&bar->s_full[i]);
     };
-    int nq = 0, at = 0;                    // items and steps so far
-    int done0 = 0, done1 = 0;              // steps of either tile
+    int n = past.plans, nq = past.items, at = past.steps;      // items and steps so far
+    int done0 = at, done1 = past.own;      // steps of either tile
     bool ok = true;
-    for (int n = 0; ok; ++n) {
+    for (; ok; ++n) {
       const Plan* plan = take(n);
       if (plan == nullptr) break;
       // (known to be the same for all lanes: the loop and the descriptors stay in uniform registers)
@@ -391,6 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    give_back(n);                          // (the end)
+    past = Past{n + 1, nq, at, done1};
     if (*abort_flag && lane == 0) {        // the products issued so far end before the CTA does
       umma_commit(&bar->drain);
       const uint64_t t0 = globaltimer_ns();
@@ -407,14 +569,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_tok = row / group, row_head = row - row_tok * group;
     // tokens of this warp's rows, behind the tile's first
     const int warp_lo = (warp & 3) * 32 / group, warp_hi = ((warp & 3) * 32 + 31) / group;
-    int done = 0;                          // steps of this tile so far
+    int n = past.plans, done = past.own;   // steps of this tile so far
+    int cared = 0;                         // items whose tiles were cleared
     bool ok = true;
-    for (int n = 0; ok; ++n) {
+    for (; ok; ++n) {
       const Plan* at = take(n);
       if (at == nullptr) break;
       const Plan plan = *at;
       give_back(n);
-      if (plan.tiles <= i) continue;
+      if (plan.tiles <= i) {
+        if (CARE) {                        // (no warp runs ahead of what has been noted)
+          ok = warp_wait(&care->noted, cared++ & 1, abort_flag);
+          if (lane == 0) mbar_arrive(&care->read);
+        }
+        continue;
+      }
       Block blk;
       blk.sink_end = plan.sink_end;
       blk.sink_cols = plan.sink_cols;
@@ -426,12 +595,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (rows of no token hold what is left in shared memory: they never raise m, which is their warp's
       // decision for all of its rows)
       float m = row < group * tpt && tok < plan.len ? -INFINITY : INFINITY, l = 0.f;
+      int partly = 0;                      // tiles that some of the item's rows do not see whole
+      uint32_t kinds = 0u;
+      if (CARE && i == 0 && cared > 0) {   // (what was noted of the last item has been read)
+        ok = warp_wait(&care->read, (cared - 1) & 1, abort_flag);
+        if (!ok) break;
+      }
       for (int j = 0; j < plan.steps; ++j, ++done) {
         ok = warp_wait(&bar->s_full[i], done & 1, abort_flag);
         if (!ok) break;
         tc_fence_after_sync();
         const int u = (plan.from + j) * kTile;
         const bool all = seen.all(u, kTile);
+        if (CARE) {                        // tile 0's warps clear V before its first product
+          const bool whole = seen_by_all(p, blk, plan.tok0, plan.tok0 + plan.tiles * tpt - 1, u);
+          if (i == 0) {
+            ok = warp_wait(&bar->v_full[done % kStages], (done / kStages) & 1, abort_flag);
+            if (!ok) break;
+            uint32_t rest = 0u;
+            const uint32_t found =
+                clear_rows<BF16>(sv + (done % kStages) * kOperand + (warp & 3) * 32 * 128, whole ? &kinds : &rest, lane);
+            if (!whole && lane == 0) {
+              care->column[min(partly, kPartly - 1)] = u;
+              care->keys[min(partly, kPartly - 1)][warp & 3] = found;
+            }
+            if (j + 1 == plan.steps) {
+              const uint32_t k = kinds | __shfl_xor_sync(0xffffffffu, kinds, 16);
+              if (lane < 16)
+                for (int e = 0; e < 3; ++e) care->kinds[warp & 3][e][lane] = static_cast<uint8_t>(k >> (8 * e));
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&care->noted);
+            }
+          }
+          if (!whole) ++partly;
+        }
         float top = -INFINITY;
 #pragma unroll 1
         for (int q = 0; q < kTile; q += 64) {          // 64 columns at a time
@@ -519,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // cycles
       if (!ok || !warp_wait(&bar->o_done[i], (done - 1) & 1, abort_flag)) break;
       tc_fence_after_sync();
-      if (plan.part.parts > 1) {
+      if (!CARE && plan.part.parts > 1) {
         // the part goes to the workspace; the last one's warps bring the sum of all back to O
         auto slot = [&](int k) {
           return slots + (static_cast<int64_t>(plan.part.slot(k)) * 2 + i) * kTilePartFloats;
@@ -595,16 +792,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
       }
-      const bool mine = row < group * tpt && tok < plan.len;
+      if (CARE) {
+        ok = warp_wait(&care->noted, cared++ & 1, abort_flag);
+        if (!ok) break;
+        add_cleared<BF16>(p, blk, care, min(partly, kPartly),
+                          static_cast<const typename H::T*>(p.v) + (plan.row0 * p.Nk + plan.hk) * kHeadDim,
+                          row < group * tpt && tok < plan.len, tok, to);
+        if (lane == 0) mbar_arrive(&care->read);
+      }
+      const bool mine = row < group * tpt && tok < plan.len && (!CARE || (plan.part.first >> i) & 1);
       const int h = plan.hk * group + row_head;
       const float inv = 1.f / l;           // (a row sees itself at least)
       const int64_t at_out = mine ? ((plan.row0 + tok) * p.Nq + h) * kHeadDim : -1;
       int64_t to_out[8];                   // of the rows that this lane stores a piece of
 #pragma unroll
       for (int k = 0; k < 8; ++k) to_out[k] = __shfl_sync(0xffffffffu, at_out, 4 * k + (lane >> 3));
-      uint8_t* stage = staged + (warp - 4) * kStage;
-      const float2 inv2 = make_float2(inv, inv), zero2 = make_float2(0.f, 0.f);
-      float2 odd[2] = {make_float2(l * 0.f, 0.f), zero2};      // NaN if anything is not finite
+      uint8_t* stage = sm.staged + (warp - 4) * kStage;
+      const float2 inv2 = make_float2(inv, inv);
+      uint32_t odd = 0u;                   // NaN if anything is not finite
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t o[2][32];
@@ -618,9 +823,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e) {
             const uint32_t* x = &o[k >> 2][(k & 3) * 8 + 2 * e];
             const float2 v = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
-            odd[e & 1] = fma_x2(v, zero2, odd[e & 1]);
             const float2 y = mul_x2(v, inv2);
             w[e] = H::pack(y.x, y.y);
+            odd = fma_16x2<BF16>(w[e], 0u, odd);
           }
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
               make_uint4(w[0], w[1], w[2], w[3]);
@@ -637,20 +842,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       tc_fence_before_sync();              // O is read before the next item's first P is announced
-      unsigned again = __ballot_sync(0xffffffffu, mine && !((odd[0].x + odd[0].y) + (odd[1].x + odd[1].y) == 0.f));
-      __syncwarp();                        // the row's own stores before the warp's
-      while (again) {
-        const int src = __ffs(again) - 1;
-        again &= again - 1;
-        const int t = __shfl_sync(0xffffffffu, tok, src), head = __shfl_sync(0xffffffffu, h, src);
-        attn_row<BF16>(p, plan.row0, t, head, lane);
+      if (!CARE) {
+        const bool spoilt = mine && l < INFINITY && (odd & 0x7fff7fffu) != 0u;
+        if (__any_sync(0xffffffffu, spoilt) && lane == 0) {
+          const int mark = n % kMarks;
+          atomicOr(&care->marks[mark >> 4], 1u << (2 * (mark & 15) + i));
+          care->marked = 1u;
+        }
       }
     }
+    give_back(n);                          // (the end)
+    past = Past{n + 1, 0, 0, done};
   }
+  return past;
+}
+
+template <bool BF16>
+__device__ __noinline__ void walk_again(const CUtensorMap* q, const CUtensorMap* k, const CUtensorMap* v,
+                                        const CUtensorMap* k8, const CUtensorMap* v8, const AttnParams* at,
+                                        uint8_t* smem_raw, int tpt, int most, bool may_split, Past past) {
+  const Smem sm = smem_of(smem_raw);
+  const AttnParams& p = *at;
+  walk<BF16, true>(Maps{q, k, v, k8, v8}, p, sm, items_of(p, sm, tpt, most, may_split), tpt, nullptr, nullptr, past);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
+                       const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ CUtensorMap tmK8,
+                       const __grid_constant__ CUtensorMap tmV8, const __grid_constant__ AttnParams p, int tpt,
+                       int most, int may_split, float* slots, uint32_t* arrived) {
+  using H = Half16<BF16>;
+  extern __shared__ uint8_t smem_raw[];
+  const Smem sm = smem_of(smem_raw);
+  Bars* bar = sm.bar;
+  volatile int* abort_flag = &bar->abort;
+  // (the shuffle tells the compiler that the warp's index is the same for all its lanes)
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+    mbar_init(&bar->q_full, 1);
+    mbar_init(&bar->q_empty, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar->k_full[i], 1);
+      mbar_init(&bar->k_empty[i], 1);
+      mbar_init(&bar->v_full[i], 1);
+      mbar_init(&bar->v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->s_full[i], 1);
+      mbar_init(&bar->p_full[i][0], kTile);
+      mbar_init(&bar->p_full[i][1], kTile);
+      mbar_init(&bar->o_done[i], 1);
+      mbar_init(&bar->parted[i], kTile);
+    }
+    mbar_init(&bar->drain, 1);
+    for (int i = 0; i < kPlans; ++i) {
+      mbar_init(&bar->plan_full[i], 1);
+      mbar_init(&bar->plan_empty[i], kReaders);
+    }
+    mbar_init(&sm.care->noted, 4);
+    mbar_init(&sm.care->read, 8);
+    sm.care->marked = 0u;
+    bar->abort = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 3)
+    for (int i = lane; i < 2 * kMarks / 32; i += 32) sm.care->marks[i] = 0u;
+  if (warp == 1) {
+    tmem_alloc(&bar->tmem, 512);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  if (p.rag.B <= kCountedSeqs) count_blocks(p.rag, tpt, sm.first);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.rag.B; i += kThreads)
+      if (seq_rows(p.rag, i).bad) atomicOr(p.err, kErrIndexRange);
+
+  const Past past = walk<BF16, false>(Maps{&tmQ, &tmK, &tmV, &tmK8, &tmV8}, p, sm, items_of(p, sm, tpt, most, may_split), tpt, slots, arrived, Past{});
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (sm.care->marked != 0u && *abort_flag == 0) {
+    walk_again<BF16>(&tmQ, &tmK, &tmV, &tmK8, &tmV8, &p, smem_raw, tpt, most, may_split, past);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+  }
+  if (warp == 1) tmem_dealloc(bar->tmem, 512);
   if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, kErrTimeout);
 }
 

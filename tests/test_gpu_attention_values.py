@@ -8,9 +8,9 @@ import torch
 import oracle
 import qkv_attention_prolog_gb300 as pkg
 from tests.attention_util import (D, SCALE, assert_within, attn_tolerance, prompts, ragged, run_paged,
-                                  run_window, to_dev)
+                                  run_window, to_dev, workspace)
 from tests.gpu_util import f64
-from tests.test_gpu_attention import _check_paged
+from tests.test_gpu_attention import _check_paged, _max_dot
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +164,114 @@ def test_rows_of_no_token_do_not_reach_the_others_bits(kind):
         got.append(d["out"][:end].clone())
     for other in got[1:]:
         assert torch.equal(got[0].view(torch.int16), other.view(torch.int16))
+
+
+# ------------------------------------------------------------------------------ values of prompts
+def _check_window_kinds(t, max_new, window=0, sinks=0):
+    """Finite outputs within the tolerance; where the oracle has a NaN or an infinity, the same one."""
+    with np.errstate(invalid="ignore"):
+        ref = oracle.window_attention(f64(t["q"]), f64(t["k"]), f64(t["v"]), t["cu_seqlens"].numpy(), SCALE,
+                                      window, sinks, out=f64(t["out"]))
+    d = to_dev(t)
+    assert run_window(d, max_new, window, sinks) == 0
+    got, want = f64(d["out"]), ref["out"]
+    ok = np.isfinite(want)
+    odd = np.where(ok, 0.0, want)
+    assert np.array_equal(np.where(np.isfinite(got), 0.0, got), odd, equal_nan=True)
+    fin = lambda x: np.nan_to_num(f64(x), nan=0, posinf=0, neginf=0)
+    with np.errstate(invalid="ignore"):
+        tol = attn_tolerance(ref, None, _max_dot(fin(t["q"]), fin(t["k"])), t["q"].dtype, t["q"].dtype, max_new)
+    rows = int(t["cu_seqlens"][-1])
+    tol[rows:] = 0
+    assert_within(np.where(ok, got, 0), np.where(ok, want, 0), np.where(ok, tol, 0), "out")
+    first = d["out"].clone()
+    assert run_window(d, max_new, window, sinks) == 0
+    assert torch.equal(first.view(torch.int16), d["out"].view(torch.int16))
+    return ok[:rows]
+
+
+KINDS = [float("nan"), float("inf"), -float("inf")]
+ODD = [  # new, Nq, Nk, window, sinks
+    ([260, 140], 3, 1, 0, 0),
+    ([260, 140], 3, 1, 70, 3),
+    ([500], 1, 1, 100, 17),                           # one head a tile: the most tokens
+    ([500], 1, 1, 300, 9),
+    ([700], 2, 2, 33, 650),                           # sinks beyond the windows of most rows
+    ([90, 7, 33], 64, 2, 20, 4),
+    ([1, 2, 130], 8, 2, 1, 0),
+    ([2100, 40], 3, 1, 0, 0),                         # items in parts
+    ([2300], 2, 1, 1700, 40),
+    ([1 + b * 7 % 40 for b in range(300)], 2, 1, 16, 2),
+]
+
+
+@pytest.mark.parametrize("new,Nq,Nk,window,sinks", ODD)
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_window_values_that_are_not_finite(new, Nq, Nk, window, sinks, dtype):
+    # single elements here and there, some channels of some rows stay finite
+    t = prompts(new, Nk, Nq, dtype, seed=66, pad=40)
+    g = torch.Generator().manual_seed(1)
+    total = sum(new)
+    for n in ("q", "k", "v"):
+        t[n][total:] = float("nan")
+    for kind in KINDS:
+        for _ in range(max(1, total // 90)):
+            at = [int(torch.randint(0, m, (1,), generator=g)) for m in (total, Nk, D)]
+            t["v"][at[0], at[1], at[2]] = kind
+    ok = _check_window_kinds(t, max(new), window, sinks)
+    assert ok.any() and not ok.all()
+
+
+@pytest.mark.parametrize("new,Nq,Nk,window,sinks", ODD[:5] + ODD[7:9])
+def test_window_channels_and_stretches_that_are_not_finite(new, Nq, Nk, window, sinks):
+    t = prompts(new, Nk, Nq, BF, seed=67)
+    t["v"][:, 0, 5] = float("nan")                    # everywhere: each row sees its own
+    t["v"][:, 0, 6] = float("inf")
+    t["v"][::2, 0, 127] = float("-inf")
+    _check_window_kinds(t, max(new), window, sinks)
+    t["v"][new[0] // 2:new[0] // 2 + 60] = float("inf")
+    t["v"][new[0] - 9:] = float("nan")
+    _check_window_kinds(t, max(new), window, sinks)
+    t["v"][:] = float("nan")
+    assert not _check_window_kinds(t, max(new), window, sinks).any()
+
+
+@pytest.mark.parametrize("new,Nq,Nk,window,sinks", ODD[:5] + ODD[7:9])
+def test_window_keys_and_queries_that_are_not_finite(new, Nq, Nk, window, sinks):
+    t = prompts(new, Nk, Nq, FP, seed=68)
+    t["k"][new[0] // 3, 0, 9] = float("nan")
+    t["k"][new[0] // 2, 0, 8] = float("inf")          # a weight of 0, or no finite one
+    t["k"][new[0] - 2, 0, 8] = float("-inf")
+    t["q"][5, 0, 0] = float("nan")
+    t["v"][new[0] // 4, 0, 3] = float("nan")
+    ok = _check_window_kinds(t, max(new), window, sinks)
+    assert ok.any() and not ok.all()
+
+
+def _window_ms(t, max_new, window=0, sinks=0):
+    d = to_dev(t)
+    a = pkg.make_window_attention_args(d, max_new, SCALE, window, sinks)
+    ws = workspace(pkg.mlap_window_attention_get_workspace_size(a))
+    best = float("inf")
+    for _ in range(4):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        pkg.mlap_window_attention_execute(a, ws)
+        end.record()
+        torch.cuda.synchronize()
+        best = min(best, start.elapsed_time(end))
+    assert pkg.mlap_check_errors(ws) == 0
+    return best
+
+
+@pytest.mark.parametrize("name,first,last,value", [
+    ("k", 0, 1, "nan"), ("v", 0, 1, "nan"), ("v", 0, 2000, "nan"), ("v", 1000, 4000, "nan"), ("v", 0, 4096, "inf")])
+def test_window_time_does_not_hang_on_what_is_not_finite(name, first, last, value):
+    # A second turn of an item costs the first one's time, clearing a tile about as long again, and a
+    # row's look at the keys around its own, 127 of them, 128 channels each, about 75 us beside the call's
+    # 55: five times the call, whatever V holds.  Rows worked out key by key, 4096 of 8 heads, are a
+    # hundred times that.
+    t = prompts([4096], 2, 8, BF, seed=69)
+    clean = _window_ms(t, 4096)
+    t[name][first:last] = float(value)
+    assert _window_ms(t, 4096) < 12 * clean
