@@ -271,6 +271,8 @@ mlap_status_t qkvrnrc_execute(const qkvrnrc_args_t* args, void* workspace,
  *     [-1, BlockNum) and a position beyond MaxBlocks * BlockSize are skipped too (append: the
  *     token's k and v are not stored; attention: the key is not visible).  Each latches
  *     MLAP_ERR_INDEX_RANGE (mlap_check_errors).  Page -1 is skipped silently.
+ *   - Lengths, tables and scales may begin at any element (a slice of a longer tensor); the other
+ *     tensors begin on 16 bytes.
  *   - Results are bitwise deterministic for a given device and arguments.  No kernel of these
  *     calls reads an input before the kernel that precedes the call in the stream has finished.
  *   - Workspaces as for mlap_execute: initialised once (mlap_workspace_init), then shared by any

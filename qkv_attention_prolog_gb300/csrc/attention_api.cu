@@ -27,7 +27,7 @@ mlap_status_t check_cache_mode(const char* mode) {
 
 // cu_seqlens (B+1) and max_new of T token rows
 mlap_status_t check_ragged(const mlap_tensor_t& cu, int64_t T, int64_t max_new, Ragged* r) {
-  CHECK_STATUS(need(cu, "cu_seqlens", false));
+  CHECK_STATUS(need(cu, "cu_seqlens", false, sizeof(int64_t)));
   CHECK_STATUS(want_dtype(cu, "cu_seqlens", MLAP_DTYPE_INT64));
   if (cu.ndim != 1 || cu.shape[0] < 1) return fail(MLAP_ERR_SHAPE, "cu_seqlens must be (B+1)");
   if (T > kMaxTokens) return fail(MLAP_ERR_UNSUPPORTED, "too many tokens");
@@ -47,10 +47,10 @@ mlap_status_t check_pages(const mlap_tensor_t& ctx, const mlap_tensor_t& table,
                           const mlap_tensor_t& kc, const mlap_tensor_t& vc,
                           const mlap_tensor_t& ks, const mlap_tensor_t& vs, int64_t Nk, Ragged* r,
                           Pages* pg) {
-  CHECK_STATUS(need(ctx, "context_lens", true));
+  CHECK_STATUS(need(ctx, "context_lens", true, sizeof(int64_t)));
   CHECK_STATUS(want_dtype(ctx, "context_lens", MLAP_DTYPE_INT64));
   CHECK_STATUS(want_shape(ctx, "context_lens", {r->B}));
-  CHECK_STATUS(need(table, "block_table", true));
+  CHECK_STATUS(need(table, "block_table", true, sizeof(int64_t)));
   CHECK_STATUS(want_dtype(table, "block_table", MLAP_DTYPE_INT64));
   if (table.ndim != 2 || table.shape[0] != r->B)
     return fail(MLAP_ERR_SHAPE, "block_table must be (B, MaxBlocks)");
@@ -64,8 +64,8 @@ mlap_status_t check_pages(const mlap_tensor_t& ctx, const mlap_tensor_t& table,
   CHECK_STATUS(want_shape(kc, "k_cache", {num, bs, Nk, kHeadDim}));
   CHECK_STATUS(want_shape(vc, "v_cache", {num, bs, Nk, kHeadDim}));
   if (bs <= 0 || bs % 16) return fail(MLAP_ERR_UNSUPPORTED, "BlockSize must be a positive multiple of 16");
-  CHECK_STATUS(need(ks, "k_scale", true));
-  CHECK_STATUS(need(vs, "v_scale", true));
+  CHECK_STATUS(need(ks, "k_scale", true, sizeof(float)));
+  CHECK_STATUS(need(vs, "v_scale", true, sizeof(float)));
   CHECK_STATUS(want_dtype(ks, "k_scale", MLAP_DTYPE_FP32));
   CHECK_STATUS(want_dtype(vs, "v_scale", MLAP_DTYPE_FP32));
   CHECK_STATUS(want_shape(ks, "k_scale", {num, Nk}));

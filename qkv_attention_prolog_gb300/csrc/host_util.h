@@ -50,14 +50,16 @@ inline std::string shape_str(const mlap_tensor_t& t) {
 
 inline bool present(const mlap_tensor_t& t) { return t.data != nullptr; }
 
-inline mlap_status_t need(const mlap_tensor_t& t, const char* name, bool allow_empty) {
+// align: bytes that the kernels read or write of the tensor at a time.
+inline mlap_status_t need(const mlap_tensor_t& t, const char* name, bool allow_empty, unsigned align = 16) {
   if (t.ndim < 0 || t.ndim > 4) return fail(MLAP_ERR_SHAPE, std::string(name) + ": ndim out of range");
   for (int i = 0; i < t.ndim; ++i)
     if (t.shape[i] < 0) return fail(MLAP_ERR_SHAPE, std::string(name) + ": negative dimension");
   if (t.data == nullptr && !(allow_empty && numel(t) == 0))
     return fail(MLAP_ERR_NULL, std::string(name) + " is NULL");
-  if (t.data != nullptr && (reinterpret_cast<uintptr_t>(t.data) & 15u) != 0)
-    return fail(MLAP_ERR_UNSUPPORTED, std::string(name) + ": data pointer not 16-byte aligned");
+  if (t.data != nullptr && (reinterpret_cast<uintptr_t>(t.data) & (align - 1)) != 0)
+    return fail(MLAP_ERR_UNSUPPORTED,
+                std::string(name) + ": data pointer not " + std::to_string(align) + "-byte aligned");
   return MLAP_OK;
 }
 

@@ -296,3 +296,21 @@ def test_workspaces_of_the_attention_calls():
     assert size("window_attention", 5000) == many
     assert size("window_attention", 5000, window=200) == 256
     assert size("window_attention", 5000, B=100) == 256
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_lengths_tables_and_scales_begin_at_any_element(op):
+    names = set(OPS[op][1])
+    for name, size in (("cu_seqlens", 8), ("context_lens", 8), ("block_table", 8), ("k_scale", 4),
+                       ("v_scale", 4)):
+        if name not in names:
+            continue
+        t = _tensors()
+        t[name].addr += size                          # as context_lens[1:] of a longer batch
+        assert _status(op, t)[0] == 0, (name, _lib.load().mlap_last_error())
+        t[name].addr += size // 2
+        assert _status(op, t)[0] == UNSUPPORTED, name
+    for name in names & {"q", "k", "v", "qkv", "cos", "sin", "out", "q_out", "k_cache", "v_cache"}:
+        t = _tensors()
+        t[name].addr += 8
+        assert _status(op, t)[0] == UNSUPPORTED, name

@@ -7,8 +7,8 @@ import torch
 
 import oracle
 import qkv_attention_prolog_gb300 as pkg
-from tests.attention_util import (D, SCALE, assert_within, attn_tolerance, prompts, ragged, run_paged,
-                                  run_window, to_dev, workspace)
+from tests.attention_util import (D, SCALE, assert_within, attn_tolerance, prompts, ragged, run_append,
+                                  run_paged, run_window, to_dev, workspace)
 from tests.gpu_util import f64
 from tests.test_gpu_attention import _check_paged, _max_dot
 
@@ -164,6 +164,28 @@ def test_rows_of_no_token_do_not_reach_the_others_bits(kind):
         got.append(d["out"][:end].clone())
     for other in got[1:]:
         assert torch.equal(got[0].view(torch.int16), other.view(torch.int16))
+
+
+# ------------------------------------------------------------------------------- places of tensors
+@pytest.mark.parametrize("new", [1, 12, 70])
+def test_lengths_tables_and_scales_of_longer_tensors(new):
+    # a batch's part that begins anywhere: appended and attended over as if it were alone
+    t = ragged([new, new], [300, 77], 16, 1, 4, BF, seed=74, width=37)
+    want, got = to_dev(t), to_dev(t)
+    for name, lead in (("cu_seqlens", 1), ("context_lens", 3), ("block_table", 1), ("k_scale", 3), ("v_scale", 1)):
+        x = want[name].reshape(-1)
+        got[name] = torch.cat([x.new_full((lead,), 99), x])[lead:].view(want[name].shape)
+        assert got[name].data_ptr() % 16 != 0 and got[name].is_contiguous()
+    for d in (want, got):
+        assert run_append(d, 4, 1, new) == 0
+        assert run_paged(d, new) == 0
+    for name in ("q_out", "out", "k_cache", "v_cache", "k_scale", "v_scale"):
+        assert torch.equal(want[name], got[name]), name
+    p = prompts([40, 90], 1, 4, BF, seed=75)
+    want, got = to_dev(p), to_dev(p)
+    got["cu_seqlens"] = torch.cat([want["cu_seqlens"][:1], want["cu_seqlens"]])[1:]
+    assert run_window(want, 90) == 0 and run_window(got, 90) == 0
+    assert torch.equal(want["out"], got["out"])
 
 
 # ------------------------------------------------------------------------------ values of prompts
