@@ -343,7 +343,7 @@ typedef struct {
   int64_t max_new;
   int64_t window;             /* >= 0; 0: every earlier key is visible */
   int64_t sinks;              /* >= 0 first positions that stay visible */
-  double softmax_scale;       /* finite */
+  double softmax_scale;       /* finite; softmax_scale * log2(e) within fp32's range */
   const char* cache_mode;     /* NULL or "PA_BSND" */
 } mlap_paged_attention_args_t;
 
@@ -366,7 +366,7 @@ typedef struct {
   int64_t max_new;
   int64_t window;             /* >= 0; 0: every earlier key is visible */
   int64_t sinks;              /* >= 0 first positions that stay visible */
-  double softmax_scale;       /* finite */
+  double softmax_scale;       /* finite; softmax_scale * log2(e) within fp32's range */
 } mlap_window_attention_args_t;
 
 mlap_status_t mlap_window_attention_get_workspace_size(const mlap_window_attention_args_t* args,

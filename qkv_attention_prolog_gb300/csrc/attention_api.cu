@@ -108,7 +108,8 @@ mlap_status_t check_attn(const mlap_tensor_t& q, const mlap_tensor_t& out, int64
   CHECK_STATUS(want_dtype(out, "out", q.dtype));
   CHECK_STATUS(want_shape(out, "out", {q.shape[0], q.shape[1], kHeadDim}));
   if (window < 0 || sinks < 0) return fail(MLAP_ERR_SHAPE, "window and sinks must not be negative");
-  if (!std::isfinite(scale)) return fail(MLAP_ERR_SHAPE, "softmax_scale must be finite");
+  const float scale_log2 = static_cast<float>(scale * 1.4426950408889634074);     // log2(e)
+  if (!std::isfinite(scale_log2)) return fail(MLAP_ERR_SHAPE, "softmax_scale must be finite, in 32 bits too");
   const int64_t most = 0x7fffffff;                       // beyond every position
   p->q = q.data;
   p->out = out.data;
@@ -116,7 +117,7 @@ mlap_status_t check_attn(const mlap_tensor_t& q, const mlap_tensor_t& out, int64
   p->Nk = static_cast<int32_t>(Nk);
   p->window = window >= most ? 0 : static_cast<int32_t>(window);
   p->sinks = static_cast<int32_t>(sinks < most ? sinks : most);
-  p->scale_log2 = static_cast<float>(scale * 1.4426950408889634074);   // log2(e)
+  p->scale_log2 = scale_log2;
   p->bf16 = q.dtype == MLAP_DTYPE_BF16;
   return MLAP_OK;
 }

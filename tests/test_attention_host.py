@@ -314,3 +314,12 @@ def test_lengths_tables_and_scales_begin_at_any_element(op):
         t = _tensors()
         t[name].addr += 8
         assert _status(op, t)[0] == UNSUPPORTED, name
+
+
+@pytest.mark.parametrize("op", ["paged_attention", "window_attention"])
+def test_refuses_scales_beyond_32_bits(op):
+    # fp32 ends below 3.41e38, and the kernels count in powers of two: 2.36e38 * log2(e)
+    for scale in (1e300, -1e39, 2.4e38):
+        assert _status(op, _tensors(), softmax_scale=scale)[0] == SHAPE, scale
+    for scale in (2.3e38, -2.3e38, 1e-300, 0.0):
+        assert _status(op, _tensors(), softmax_scale=scale)[0] == 0, scale
