@@ -49,13 +49,11 @@ SHAPES = [(1, 16, 2, FEW), (4, 8, 2, FEW), (70, 8, 2, TILES)]
 
 # ---------------------------------------------------------------------------------------- queries
 @pytest.mark.parametrize("new,Nq,Nk,size", SHAPES)
-@pytest.mark.parametrize("dtype", [BF, FP])
-@pytest.mark.parametrize("loud", [float("inf"), float("nan"), 2.0 ** 40, 2.0 ** 13])
+@pytest.mark.parametrize("dtype,loud", [(BF, float("inf")), (BF, float("nan")), (BF, 2.0 ** 40), (BF, 2.0 ** 13),
+                                        (FP, float("inf")), (FP, float("nan")), (FP, 2.0 ** 13)])
 def test_paged_rows_do_not_depend_on_each_other(new, Nq, Nk, size, dtype, loud):
     # one row of a tile holds an infinity, a NaN or values far above the others': the others' outputs
     # are those of their own scores
-    if loud == 2.0 ** 40 and dtype == FP:
-        pytest.skip("no fp16 value")
     t = ragged([new, new], [90, 333], 16, Nk, Nq, dtype, seed=61)
     ordinary = f64(t["q"]).copy()
     if np.isfinite(loud):
@@ -188,6 +186,23 @@ def test_lengths_tables_and_scales_of_longer_tensors(new):
     assert torch.equal(want["out"], got["out"])
 
 
+def test_paged_batch_in_two_calls_on_slices():
+    # single tokens and a prompt's chunk, each by the kernel meant for it, into one output
+    t = ragged([1, 1, 1, 70], [900, 4, 333, 200], 16, 2, 8, FP, seed=76, width=61)
+    ref = _oracle_paged(t)
+    d = to_dev(t)
+    for lo, hi, new, size in ((0, 3, 1, FEW), (3, 4, 70, TILES)):
+        part = dict(d, cu_seqlens=d["cu_seqlens"][lo:hi + 1], context_lens=d["context_lens"][lo:hi],
+                    block_table=d["block_table"][lo:hi])
+        _takes(part, new, size)
+        assert run_paged(part, new) == 0
+    tol = attn_tolerance(ref, None, np.abs(f64(t["q"])).max() * 127.0 * float(t["k_scale"].max()) * D * SCALE, FP, FP,
+                         _keys(t))
+    rows = int(t["cu_seqlens"][-1])
+    assert_within(f64(d["out"])[:rows], ref["out"][:rows], tol[:rows], "out")
+    assert bool((d["out"][rows:] == 7).all())
+
+
 # ------------------------------------------------------------------------------ values of prompts
 def _check_window_kinds(t, max_new, window=0, sinks=0):
     """Finite outputs within the tolerance; where the oracle has a NaN or an infinity, the same one."""
@@ -267,6 +282,19 @@ def test_window_keys_and_queries_that_are_not_finite(new, Nq, Nk, window, sinks)
     t["q"][5, 0, 0] = float("nan")
     t["v"][new[0] // 4, 0, 3] = float("nan")
     ok = _check_window_kinds(t, max(new), window, sinks)
+    assert ok.any() and not ok.all()
+
+
+def test_window_more_items_than_marks():
+    # 160 short prompts of 256 heads: 269 items for each of 152 blocks, which keeps 256 marks
+    Nk = 256
+    t = prompts([1 + b % 3 for b in range(160)], Nk, Nk, FP, seed=77)
+    g = torch.Generator().manual_seed(2)
+    for _ in range(60):
+        row, head, ch = (int(torch.randint(0, m, (1,), generator=g)) for m in (t["v"].shape[0] - 2, Nk, D))
+        t["v"][row, head, ch] = float("nan")
+    t["v"][2, :, 7] = float("inf")                    # (the second prompt's last token, in every head)
+    ok = _check_window_kinds(t, 3)
     assert ok.any() and not ok.all()
 
 
