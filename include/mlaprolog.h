@@ -264,7 +264,9 @@ mlap_status_t qkvrnrc_execute(const qkvrnrc_args_t* args, void* workspace,
  *     BlockSize at most 2^30.  -1 stands for no page.
  *   - Caches (BlockNum, BlockSize, Nk, D) int8 with one fp32 scale for each page and head
  *     (BlockNum, Nk): the cached value is code * scale (attention counts a v_scale below 2^-90 in
- *     magnitude as 0).  D = 128; Nq is a multiple of Nk, query
+ *     magnitude as 0).  They are written by mlap_kv_append_execute alone: the QKV entry's caches have
+ *     scales of another shape.  Nor does append return the rotated keys in 16 bits; for prompts that
+ *     attend over their own, the QKV entry does (k_before_quant).  D = 128; Nq is a multiple of Nk, query
  *     head h reads head h / (Nq/Nk) of the cache.
  *   - A sequence whose cu_seqlens entries are out of order or out of [0, T], that has more than
  *     max_new tokens or a context_lens outside [0, 2^29] is skipped; a page id outside
@@ -273,6 +275,8 @@ mlap_status_t qkvrnrc_execute(const qkvrnrc_args_t* args, void* workspace,
  *     MLAP_ERR_INDEX_RANGE (mlap_check_errors).  Page -1 is skipped silently.
  *   - Lengths, tables and scales may begin at any element (a slice of a longer tensor); the other
  *     tensors begin on 16 bytes.
+ *   - Softmax weights enter the second product in 16 bits: bf16 in window attention of bf16 tensors,
+ *     else fp16; their maxima, their sums and all accumulators are fp32.
  *   - Results are bitwise deterministic for a given device and arguments.  No kernel of these
  *     calls reads an input before the kernel that precedes the call in the stream has finished.
  *   - Workspaces as for mlap_execute: initialised once (mlap_workspace_init), then shared by any
@@ -329,7 +333,9 @@ mlap_status_t mlap_kv_append_execute(const mlap_kv_append_args_t* args, void* wo
  *   out[row, h] = sum over visible t of softmax_t(softmax_scale * q . k[t]) v[t],
  *   t is visible to a query at position p when t <= p, p - t < window (window 0: no limit) or
  *   t < sinks, and its page is valid.  A query that sees no key gets a row of zeros.
- * From one query per sequence (decode) through a few (drafts) to chunks of a prompt. */
+ * From one query per sequence (decode) through a few (drafts) to chunks of a prompt.  max_new chooses
+ * the kernel of all of a call's sequences: a batch of single tokens and a prompt's chunk takes half the
+ * time as two calls, on slices of cu_seqlens, context_lens and block_table. */
 typedef struct {
   mlap_tensor_t q;            /* fp16|bf16 (T, Nq, D) */
   mlap_tensor_t k_cache;      /* int8 (BlockNum, BlockSize, Nk, D) */

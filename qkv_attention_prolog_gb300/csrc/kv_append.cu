@@ -17,7 +17,7 @@
 // Bound by memory: 16 prompts of up to 1024 tokens move 256 MB in 52 us (4.9 TB/s), pages' rows
 // coming from the L2 the second time.  Held instead in shared memory (64 KB, three CTAs on an SM)
 // they cost 56 us, in registers 97; half a row's elements in each lane (sixteen lanes a row) 71;
-// two CTAs on an SM 62, five with spilled registers 63.
+// two CTAs on an SM 62, five 63 (four spill 44 bytes a thread, 240 where warps take units).
 //
 // Every product and sum is rounded on its own (no contraction), in one fixed order, so the codes
 // are the same whole numbers that the operator's definition in 32-bit arithmetic gives.

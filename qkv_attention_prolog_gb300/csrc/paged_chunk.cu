@@ -14,7 +14,7 @@
 //                   requests an item's Q by TMA
 //   warp 15         looks up the pages and scales of the tiles' eight runs of 16 tokens, ahead
 //
-// A step (128 keys of both tiles) takes 2.2 us, and as much with one tile: it is bound by the chain
+// A step (128 keys of both tiles) takes 2.1 us, and as much with one tile: it is bound by the chain
 // score product, softmax, value product of a tile, which the other one's fills, and which the
 // expanders' instructions on the same schedulers lengthen (window_attn.cu, without them, 1.6 us).
 // Rows of no page and rows behind the sequence's end become zeros, so nothing that is masked
@@ -22,10 +22,10 @@
 //
 // Items (256 rows of a head) are dealt whole while there is one for each CTA; what is left, fewer
 // than CTAs, is split by steps, and the parts meet in the workspace.  2 x 1000 tokens over 8192,
-// 256 items: 257 us, 1.11 PFLOP/s; without the split 328 before, with it 297.  256 tokens over 50000,
-// 32 items: 196 us.  116 prompts of up to 143 tokens, 1200 items of one or two steps: 66 us; 92 with
-// bf16 queries scaled into f16's range in shared memory, 146 in registers (2 x 1000 over 8192: 255
-// and 268).
+// 256 items: 246 us, 1.16 PFLOP/s (before K's codes became q's type 297, without the split 328).  256 tokens over 50000,
+// 32 items: 187 us.  116 prompts of up to 143 tokens, items of one or two steps: 79 us; bf16 queries
+// scaled into f16's range took a third longer in shared memory, twice as long in registers (2 x 1000
+// over 8192: 255 and 268).
 // What did not pay: three expanding warps (353 us) or seven without a warp of look-ups
 // (380), other orders of the issuing warp's waits (the same).
 #include "attn_tile.cuh"
@@ -746,10 +746,10 @@ int64_t items_of(const AttnParams& p, int tpt) {
 }  // namespace
 
 // From four 16-row tiles a block on.  Both paths, this one second, 32 heads on 8:
-//   three tiles (12 tokens)   16 x 8000: 143, 120 us   64 x 2000: 156, 128   1 x 50000: 64, 82
-//                             1 x 1000: 13, 23         96 in a window of 1024: 112, 128
-//   four tiles (16 tokens)    16 x 8000: 183, 120      64 x 2000: 201, 129   1 x 1000: 14, 23
-//   six tiles (24 tokens)     16 x 8000: 267, 120      96 in a window of 1024: 197, 129
+//   three tiles (12 tokens)   16 x 8000: 136, 116 us   64 x 2000: 146, 125   1 x 50000: 59, 81
+//                             1 x 1000: 12, 21         96 in a window of 1024: 105, 122
+//   four tiles (16 tokens)    16 x 8000: 173, 116      64 x 2000: 188, 124   1 x 1000: 13, 21
+//   six tiles (24 tokens)     16 x 8000: 252, 116      96 in a window of 1024: 188, 122
 // (How long the contexts are is known on the device alone.)
 bool paged_chunk_pays(const AttnParams& p) {
   const int group = p.Nq / p.Nk, tpt = window_attn_tokens(group);

@@ -12,13 +12,14 @@
 // multiply-adds: the tensor cores' register path (mma.sync m16n8k16, 16-bit operands, fp32 sums) has
 // the rate for 8 or 16 rows, and its operands come from registers, where int8 becomes 16 bits by a
 // byte permute and one packed instruction, exactly: V's codes f16, K's the type of q, which enters the
-// first product as it is (scaled into f16's range, bf16 rows lost bits to the largest one beside them).  Both products run transposed, S^T = K q^T and
-// O^T = V^T P^T, so that the tokens and the channels fill the 16 rows of the instruction and the
-// query rows its 8 columns: eight rows (one token of up to eight heads) cost half of what rows as
-// the 16-row operand would, and P turns from the first product's layout to the second's by an 8x8
-// register transpose (movmatrix).  Each of a CTA's four warps streams its own pairs of 16-token
-// steps (the largest run of tokens that a page is sure to hold whole) by TMA into a ring of two
-// pairs, and joins the others at the end, so no barrier stands between the loads and the products.
+// first product as it is (scaled into f16's range, bf16 rows lost bits to the largest one beside
+// them).  Both products run transposed, S^T = K q^T and O^T = V^T P^T, so that the tokens and the
+// channels fill the 16 rows of the instruction and the query rows its 8 columns: eight rows (one
+// token of up to eight heads) cost half of what rows as the 16-row operand would, and P turns from
+// the first product's layout to the second's by an 8x8 register transpose (movmatrix).  Each of a
+// CTA's four warps streams its own pairs of 16-token steps (the largest run of tokens that a page
+// is sure to hold whole) by TMA into a ring of two pairs, and joins the others at the end, so no
+// barrier stands between the loads and the products.
 //
 // The work is a line of steps: sequence by sequence, row tile by row tile, head by head, in equal
 // stretches for all CTAs (three on each SM), so ragged batches and single long sequences load all
@@ -38,15 +39,17 @@
 //
 // Measured: 64 sequences of up to 8192 tokens (32 heads on 8) 98 us, 6.1 TB/s (57 of 4608, where no
 // tile is split, stream at 7.2 TB/s); one over 131071 tokens 53 us: the first product at 4.4, the
-// median block's last one at 42, the last join at the end; one over 600 tokens 8.9, of which 2 lay
+// median block's last one at 42, the last join at the end; one over 600 tokens 8.6, of which 2 lay
 // out the line, 3 come before the first product and 2 are the join (a loop over the children that
 // waited for each one's loads took 0.5 more).  Four drafted tokens of seven heads, 28
 // rows, take two tiles of 16 and read the codes twice: 96 sequences within a window of 1024 take
-// 46 us, bound by the issue of instructions (about a thousand for each pair of steps, a third of them
-// int8 to f16).  What did not pay: tiles of 32 rows (255 registers, q's fragments in shared memory,
-// two CTAs an SM): 16 x 8 tokens over 8000 100 -> 89 us, but those drafts 46 -> 59 and one sequence's
-// 8 tokens over 1000 13 -> 18; more stretches than resident CTAs (131071 tokens 69 -> 108 us, all of
-// it parts and joins); two CTAs an SM for 16-row tiles (4 tokens over 1024: 49 -> 55 us).
+// 43 us.  Nothing is full there: DRAM at a third of its rate, 42 % of the issue slots (about a thousand
+// instructions for each pair of steps, a third of them int8 to 16 bits); a tile's start and join, over a
+// quarter of the line, and the chain of a pair's two products are what is left.  What did not pay:
+// tiles of 32 rows (255 registers, q's fragments in shared memory, two CTAs an SM): 16 x 8 tokens
+// over 8000 100 -> 89 us, but those drafts 46 -> 59 and one sequence's 8 tokens over 1000 13 -> 18;
+// more stretches than resident CTAs (131071 tokens 69 -> 108 us, all of it parts and joins); two
+// CTAs an SM for 16-row tiles (4 tokens over 1024: 49 -> 55 us).
 #include "attn_common.cuh"
 #include "attn_ptx.cuh"
 #include "attn_tile.cuh"
@@ -295,8 +298,8 @@ struct Cursor {                            // where the block is on the line
 };
 
 // The cursor's start, by the thread whose sequences (the first one is b, at place begin) hold it.
-__device__ __forceinline__ void start_cursor(const AttnParams& p, const Line& l, int inner, int tile_rows,
-                                             int b, int64_t begin, SeqWork w, bool only, Cursor* cur) {
+__device__ __forceinline__ void start_cursor(const AttnParams& p, const Line& l, int tile_rows, int b,
+                                             int64_t begin, SeqWork w, bool only, Cursor* cur) {
   cur->group = static_cast<int>(blockIdx.y);
   cur->head = static_cast<int>(blockIdx.x);
   const int64_t lo = cur->group * l.share;
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_decode_kernel(
     if (lo >= l.total) return;
     if (begin <= lo && lo < begin + places) {            // one thread
       line = l;
-      start_cursor(p, l, parts.inner, kRows, threadIdx.x * per_thread, begin, w, per_thread == 1, &cur);
+      start_cursor(p, l, kRows, threadIdx.x * per_thread, begin, w, per_thread == 1, &cur);
       next_seg(p, l, parts.inner, kRows, &cur, &segs[0]);
     }
     __syncthreads();

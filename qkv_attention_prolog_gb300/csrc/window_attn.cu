@@ -26,8 +26,9 @@
 // 8192 tokens of one k/v head, 128 items: 101 us a CTA each, 67 shared.
 //
 // A step takes 1.6 us where all of a tile is visible.  One prompt of 8192 tokens (32 heads on 8, bf16)
-// 352 us, 1.56 PFLOP/s, in a window of 2048 178 us, 1.36; 16 prompts of up to 1024 in a window of
-// 256, 213 MB, 75 us: three steps an item, as long again for its start and its output.  What did
+// 355 us in short loops, 378, 1.45 PFLOP/s, in long ones; in a window of 2048 178 and 189 us, 1.28; 16
+// prompts of up to 1024 in a window of 256, 213 MB, 73 us: three steps an item, as long again for its
+// start and its output.  What did
 // not pay: two issuing warps (499 -> 540 us for 8192), a row's columns shared by two threads (377 ->
 // 504: the products then run at half their rate), waits on several barriers by one warp's lanes at
 // a time (384 -> 366 us one after another), the softmax loops unrolled (206 -> 184 us rolled, window
@@ -228,8 +229,9 @@ __device__ __noinline__ uint32_t clear_rows(uint8_t* rows, uint32_t* kinds, int 
       for (int i = 0; i < 4; ++i) {
         const uint32_t nan = odd[i] & ~__vcmpeq2(w[i] & 0x7fff7fffu, kExp * 0x10001u);
         const uint32_t neg = w[i] >> 15 & 0x00010001u, is = odd[i] & 0x00010001u, n = nan & 0x00010001u;
-        const uint32_t bits = (is & ~n & ~neg) | (is & ~n & neg) << 8;           // of the low value, and high
-        *kinds |= ((bits & 0x101u) | n << 16 & 0x10000u) << (2 * i) | (bits >> 16 | n & 0x10000u) << (2 * i + 1);
+        const uint32_t bits = (is & ~n & ~neg) | (is & ~n & neg) << 8;
+        const uint32_t low = (bits & 0x101u) | (n << 16 & 0x10000u), high = bits >> 16 | (n & 0x10000u);
+        *kinds |= low << (2 * i) | high << (2 * i + 1);
         w[i] &= ~odd[i];
       }
       *reinterpret_cast<uint4*>(at + r * 128 + (((lane & 7) ^ ((r + (lane >> 4)) & 7)) << 4)) =
@@ -613,8 +615,8 @@ __device__ __forceinline__ Past walk(const Maps& maps, const AttnParams& p, cons
             ok = warp_wait(&bar->v_full[done % kStages], (done / kStages) & 1, abort_flag);
             if (!ok) break;
             uint32_t rest = 0u;
-            const uint32_t found =
-                clear_rows<BF16>(sv + (done % kStages) * kOperand + (warp & 3) * 32 * 128, whole ? &kinds : &rest, lane);
+            uint8_t* rows = sv + (done % kStages) * kOperand + (warp & 3) * 32 * 128;
+            const uint32_t found = clear_rows<BF16>(rows, whole ? &kinds : &rest, lane);
             if (!whole && lane == 0) {
               care->column[min(partly, kPartly - 1)] = u;
               care->keys[min(partly, kPartly - 1)][warp & 3] = found;
@@ -863,7 +865,8 @@ __device__ __noinline__ void walk_again(const CUtensorMap* q, const CUtensorMap*
                                         uint8_t* smem_raw, int tpt, int most, bool may_split, Past past) {
   const Smem sm = smem_of(smem_raw);
   const AttnParams& p = *at;
-  walk<BF16, true>(Maps{q, k, v, k8, v8}, p, sm, items_of(p, sm, tpt, most, may_split), tpt, nullptr, nullptr, past);
+  walk<BF16, true>(Maps{q, k, v, k8, v8}, p, sm, items_of(p, sm, tpt, most, may_split), tpt, nullptr, nullptr,
+                   past);
 }
 
 template <bool BF16>
@@ -927,7 +930,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = threadIdx.x; i < p.rag.B; i += kThreads)
       if (seq_rows(p.rag, i).bad) atomicOr(p.err, kErrIndexRange);
 
-  const Past past = walk<BF16, false>(Maps{&tmQ, &tmK, &tmV, &tmK8, &tmV8}, p, sm, items_of(p, sm, tpt, most, may_split), tpt, slots, arrived, Past{});
+  const Past past = walk<BF16, false>(Maps{&tmQ, &tmK, &tmV, &tmK8, &tmV8}, p, sm,
+                                      items_of(p, sm, tpt, most, may_split), tpt, slots, arrived, Past{});
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
