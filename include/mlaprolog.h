@@ -275,6 +275,8 @@ mlap_status_t qkvrnrc_execute(const qkvrnrc_args_t* args, void* workspace,
  *     MLAP_ERR_INDEX_RANGE (mlap_check_errors).  Page -1 is skipped silently.
  *   - Lengths, tables and scales may begin at any element (a slice of a longer tensor); the other
  *     tensors begin on 16 bytes.
+ *   - A page whose k_scale * softmax_scale is 2^113 or more in magnitude counts as infinite in paged
+ *     attention of bf16 queries (fp16: 2^127); queries may have any finite value.
  *   - Softmax weights enter the second product in 16 bits: bf16 in window attention of bf16 tensors,
  *     else fp16; their maxima, their sums and all accumulators are fp32.
  *   - Results are bitwise deterministic for a given device and arguments.  No kernel of these
